@@ -210,13 +210,13 @@ __device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(
 __device__ __forceinline__ float exp_neg_abs(float x) { return exp2_hw(fabsf(x) * -kLog2e); }
 
 // log(1 + exp(x)) = max(x, 0) + log1p(e), e = exp_neg_abs(x); log1p by the log of the rounded sum
-// corrected by e / (rounded sum - 1), which keeps small e exact.  NaN comes
-// through.
+// corrected by e / (rounded sum - 1), which keeps small e exact.  The max is a
+// select: 0 at x = -inf (a row whose step is masked), and NaN comes through.
 __device__ __forceinline__ float softplus_e(float x, float e)
 {
     const float w = 1.0f + e, d = w - 1.0f;
     const float l = d == 0.0f ? e : __builtin_amdgcn_logf(w) * kLn2 * (e * rcp_hw(d));
-    return fmaf(0.5f, x, 0.5f * fabsf(x)) + l;
+    return (x < 0.0f ? 0.0f : x) + l;
 }
 
 // 1 / (1 + exp(-x)): the product with log2(e) is rounded once, so for negative x

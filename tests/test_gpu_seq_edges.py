@@ -1,0 +1,66 @@
+"""Sequence-block operators on the GPU where single values are not finite,
+against the fp64 oracle.  Tolerances: tests/tolerances.py."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import seq_oracle as so
+from tests.test_gpu_seq import MANY, S, dev, f64, ok, rng, say, scan_inputs, split  # noqa: F401
+from tests.tolerances import check_seq, scan_k
+
+pytestmark = pytest.mark.gpu
+
+# in rows and, with many sequences, with a channel per lane
+LAYOUTS = [([1], 1, "f32"), ([40], 1, "f16"), ([70, 9, 0, 130], 2, "bf16"), ([300], 1, "f32"), (MANY, 1, "f32"), (MANY, 2, "bf16")]
+
+
+@pytest.mark.parametrize("n,G,dtype", LAYOUTS)
+def test_scan_steps_of_minus_infinity(S, n, G, dtype):  # noqa: F811
+    """dt = -inf (a masked row) and dt_bias = -inf (a channel switched off):
+    delta = softplus(-inf) = 0, so the state is kept, and no gradient reaches
+    dt.  The oracle's values are those of -1e4, where softplus and its slope are
+    0 in fp64 too but the masses stay finite."""
+    say("scan -inf", len(n), G, dtype)
+    D, N = 6, 5
+    a, ref, where = scan_inputs(n, D, N, G, dtype)
+    r = rng(20, len(n), G)
+    rows = r.random(sum(n)) < 0.3
+    rows[-1] = True
+    off = np.arange(D) == 2
+    low, high = a["dt"].clone(), a["dt_bias"].clone()
+    a["dt"][torch.from_numpy(rows).cuda()] = -float("inf")
+    a["dt_bias"][2] = -float("inf")
+    low[torch.from_numpy(rows).cuda()] = -1e4
+    high[2] = -1e4
+    ref = ref[:1] + (f64(low),) + ref[2:7] + (f64(high),) + ref[8:]
+    with np.errstate(invalid="ignore"):
+        inf = so.selective_scan(*(ref[:1] + (f64(a["dt"]),) + ref[2:7] + (f64(a["dt_bias"]),) + ref[8:]), where)[0]
+    (y, h), (my, mh) = so.selective_scan(*ref, where)
+    assert np.array_equal(inf[0], y) and np.array_equal(inf[1], h)
+
+    args, kw = split(a)
+    x = np.where(rows[:, None] | off[None], -1e4, ref[1] + ref[7])
+    k = scan_k(x, 0.0, ref[2], True, N)
+    f = S.selective_scan_fwd(*args, save=True, **kw)
+    ok(check_seq("y", f64(f.y), y, my, dtype, k))
+    ok(check_seq("h_last", f64(f.h_last), h, mh, "f32", k))
+    dy, dh = dev(r.normal(size=y.shape), dtype), dev(r.normal(size=h.shape))
+    d = S.selective_scan_bwd(dy, *args, f.hist, dh_last=dh, **kw)
+    g, m = so.selective_scan_bwd(f64(dy), *ref, f64(dh), where)
+    for key in g:
+        ok(check_seq(key, f64(getattr(d, key)), g[key], m[key], dtype if key in ("du", "ddt", "dz", "dB", "dC") else "f32",
+                     scan_k(x, 0.0, ref[2], True, {"dB": D, "dC": D}.get(key, 16))))
+    assert not f64(d.ddt)[rows].any() and not f64(d.ddt)[:, off].any() and f64(d.ddt_bias)[2] == 0
+
+    # the same rows as single tokens: a sequence each
+    T = min(sum(n), 200)
+    one = [v if i == 2 else v[:T].contiguous() for i, v in enumerate(args)]
+    h0 = dev(r.normal(size=(T, N, D)))
+    state = h0.clone()
+    ys = S.selective_scan_step(state, *one, skip=kw["skip"], z=kw["z"][:T].contiguous(), dt_bias=kw["dt_bias"])
+    cut = [ref[0][:T], ref[1][:T], ref[2], ref[3][:T], ref[4][:T], ref[5], ref[6][:T], ref[7], ref[8], f64(h0)]
+    (y, h), (my, mh) = so.selective_scan(*cut, so.spans(T, np.arange(T + 1)))
+    ok(check_seq("y", f64(ys), y, my, dtype, k))
+    ok(check_seq("h", f64(state), h, mh, "f32", k))
+    kept = np.zeros((T, 1, D), bool) | rows[:T, None, None] | off
+    assert np.array_equal(f64(state)[np.broadcast_to(kept, state.shape)], f64(h0)[np.broadcast_to(kept, state.shape)])
