@@ -27,7 +27,8 @@
  *     result.
  *     A call whose pieces need 2^32 lanes or more in one launch is refused
  *     (a wavefront takes 16 rows of a sequence and 128 channels in the
- *     convolution, 64 rows and 64 channels of a group in the scan).
+ *     convolution, 64 rows and 64 channels of a group in the scan), and so is
+ *     a backward scan whose dB and dC have so many values (a lane sums four).
  *   - Workspaces are device memory of the size the *_workspace_bytes call
  *     gives (0 for sizes that the call itself refuses).
  */

@@ -197,6 +197,20 @@ ScanWs scan_bwd_ws(const seq_scan& a)
     return w;
 }
 
+// The backward pass's last launch, the sums of the partial gradients, has lanes
+// by the values of dB and dC as well.
+int check_scan_bwd(const char* fn, const seq_scan* a)
+{
+    SEQ_TRY(check_scan(fn, a));
+    const ScanWs w = scan_bwd_ws(*a);
+    const int64_t bc = a->total * a->G * a->N, blocks = seq::scan_bwd_blocks(a->D, a->G, w.chans);
+    const int64_t need = 2 * seq::sum_rows_blocks(blocks, bc) + seq::sum_rows_blocks(w.slots, (int64_t)a->N * a->D) +
+                         2 * seq::sum_rows_blocks(w.slots, a->D);
+    if (need >= (int64_t)1 << 24)
+        return fail(CFC_EINVAL, "%s: the gradients of %lld rows, %d groups and %d states need more workgroups than a launch has", fn, (long long)a->total, a->G, a->N);
+    return CFC_OK;
+}
+
 seq::ScanArgs scan_args(const seq_scan& a)
 {
     seq::ScanArgs k{};
@@ -483,7 +497,7 @@ size_t seq_selective_scan_fwd_workspace_bytes(const seq_scan* a)
 
 size_t seq_selective_scan_bwd_workspace_bytes(const seq_scan* a)
 {
-    if (check_scan("seq_selective_scan_bwd_workspace_bytes", a)) return 0;
+    if (check_scan_bwd("seq_selective_scan_bwd_workspace_bytes", a)) return 0;
     return sizeof(float) * (size_t)scan_bwd_ws(*a).total;
 }
 
@@ -529,7 +543,7 @@ int seq_selective_scan_bwd(const seq_scan* a, const void* dy, int64_t lddy, cons
 {
     const char* fn = "seq_selective_scan_bwd";
     cfc_host::last_error().clear();
-    SEQ_TRY(check_scan(fn, a));
+    SEQ_TRY(check_scan_bwd(fn, a));
     SEQ_TRY(check_scan_inputs(fn, *a));
     if (!g) return fail(CFC_EINVAL, "%s: the gradients are NULL", fn);
     const int dtype = a->dtype;

@@ -24,6 +24,7 @@ struct SumArgs {
     SumSeg seg[kMaxSumSegs];
     int nseg;
 };
+int64_t sum_rows_blocks(int64_t R, int64_t N);   // of 256 lanes, for one segment; a launch has fewer than 2^24
 hipError_t launch_sum_rows(SumArgs a, hipStream_t s);
 
 struct LnArgs {

@@ -474,6 +474,13 @@ hipError_t launch_ln_bwd(const LnArgs& a, hipStream_t s)
     });
 }
 
+// Workgroups of the row sum of an R x N segment.
+int64_t sum_rows_blocks(int64_t R, int64_t N)
+{
+    const int64_t cols = 256 / sum_slices(R) * 4;
+    return (N + cols - 1) / cols;
+}
+
 hipError_t launch_sum_rows(SumArgs a, hipStream_t s)
 {
     int64_t blocks = 0;
@@ -482,8 +489,7 @@ hipError_t launch_sum_rows(SumArgs a, hipStream_t s)
         SumSeg g = a.seg[i];
         if (g.N <= 0 || !g.out) continue;
         g.block0 = blocks;
-        const int64_t cols = 256 / sum_slices(g.R) * 4;
-        blocks += (g.N + cols - 1) / cols;
+        blocks += sum_rows_blocks(g.R, g.N);
         a.seg[n++] = g;
     }
     a.nseg = n;

@@ -236,3 +236,27 @@ def test_row_strides():
                       (torch.zeros(1, 8).expand(4, 8), 1)):
         with pytest.raises(TypeError):
             _row_stride(bad, "x", lead)
+
+
+def test_gradient_sums_beyond_a_grid_are_refused(L):
+    """dB and dC of 8,192 rows x 16,384 groups x 64 states are 2^34 values, four
+    to a lane of the launch that sums them: 2^32 lanes.  The forward pass has no
+    such launch; 64 rows fewer pass this check and fail at the next."""
+    from recurrent_cell_amd import seq
+
+    def bwd(a):
+        return L.seq_selective_scan_bwd(a, at(10), 16384, at(11), None, seq._ScanGrads(
+            at(14), 16384, at(15), 16384, at(16), 16384, at(17), at(19), at(21), at(22), at(23), at(24)), at(40), 1 << 40, None)
+
+    def args(rows):
+        return scan(total=rows, len=rows, n_seq=1, D=16384, G=16384, N=64, ldu=16384, lddt=16384, ldz=16384, ldb=1 << 20, ldc=1 << 20,
+                    dtype=BF16, u=None, C=at(60))
+
+    a = args(8192)
+    assert L.seq_selective_scan_bwd_workspace_bytes(a) == 0 and "workgroups" in err(L)
+    assert bwd(a) == -1 and "workgroups" in err(L)
+    assert L.seq_selective_scan_hist_floats(a) == 8192 // 64 * 64 * 16384
+    assert L.seq_selective_scan_fwd(a, at(10), 16384, None, at(11), at(40), 1 << 40, None) == -1 and "u is NULL" in err(L)
+    a = args(8192 - 64)
+    assert L.seq_selective_scan_bwd_workspace_bytes(a) > 1 << 36
+    assert bwd(a) == -1 and "u is NULL" in err(L)
