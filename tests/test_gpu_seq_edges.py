@@ -64,3 +64,45 @@ def test_scan_steps_of_minus_infinity(S, n, G, dtype):  # noqa: F811
     ok(check_seq("h", f64(state), h, mh, "f32", k))
     kept = np.zeros((T, 1, D), bool) | rows[:T, None, None] | off
     assert np.array_equal(f64(state)[np.broadcast_to(kept, state.shape)], f64(h0)[np.broadcast_to(kept, state.shape)])
+
+
+def finite_or_equal(name, x, ref, mass, dtype, k):
+    """Where the definition is finite, its bound; where it is infinite, the same
+    infinity; where it is NaN (infinities of both signs), anything."""
+    fin, inf = np.isfinite(ref), np.isinf(ref)
+    assert np.array_equal(x[inf], ref[inf]), (name, int((x[inf] != ref[inf]).sum()), "of", int(inf.sum()))
+    ok(check_seq(name, x[fin], ref[fin], mass[fin], dtype, k))
+
+
+@pytest.mark.parametrize("layout", [0, 1, 2])
+@pytest.mark.parametrize("N", [1, 3, 5, 6, 11, 12, 16, 17, 20, 33, 48])
+def test_scan_infinite_inputs(S, N, layout):  # noqa: F811
+    """An infinite u leaves what the definition makes of it: infinities, not NaN,
+    in its channel from its row on, also where N states do not fill their tile;
+    and nothing in the gradients that do not meet it."""
+    say("scan inf", N, layout)
+    n, dtype = [([40], "f32"), ([130, 7, 70], "bf16"), (MANY, "f32")][layout]
+    D, rows = 3, sum(n)
+    a, ref, where = scan_inputs(n, D, N, 1, dtype)
+    r = rng(21, N, layout)
+    # all positive, decays that stay above 0: every infinity has one sign
+    for key in ("B", "C", "z", "u"):
+        a[key] = a[key].abs() + 0.125
+    a["dt_bias"] = dev(r.uniform(-6, -5, size=D))
+    a["h0"], a["skip"] = a["h0"].abs(), a["skip"].abs()
+    dy, dh = dev(r.uniform(0.1, 1, size=(rows, D)), dtype), dev(r.uniform(0.1, 1, size=(len(n), N, D)))
+    a["u"][n[0] // 2, 0] = float("inf")
+    ref = (f64(a["u"]), ref[1], ref[2], f64(a["B"]), f64(a["C"]), f64(a["skip"]), f64(a["z"]), f64(a["dt_bias"]), True, f64(a["h0"]))
+    args, kw = split(a)
+    with np.errstate(invalid="ignore"):
+        (y, h), (my, mh) = so.selective_scan(*ref, where)
+        g, m = so.selective_scan_bwd(f64(dy), *ref, f64(dh), where)
+    assert np.isinf(y[n[0] // 2:n[0], 0]).all() and np.isfinite(y[:, 1:]).all() and np.isinf(g["dA"][:, 0]).all()
+    k = scan_k(ref[1], ref[7], ref[2], True, N)
+    f = S.selective_scan_fwd(*args, save=True, **kw)
+    finite_or_equal("y", f64(f.y), y, my, dtype, k)
+    finite_or_equal("h_last", f64(f.h_last), h, mh, "f32", k)
+    d = S.selective_scan_bwd(dy, *args, f.hist, dh_last=dh, **kw)
+    for key in g:
+        finite_or_equal(key, f64(getattr(d, key)), g[key], m[key], dtype if key in ("du", "ddt", "dz", "dB", "dC") else "f32",
+                        scan_k(ref[1], ref[7], ref[2], True, {"dB": D, "dC": D}.get(key, N)))
