@@ -212,12 +212,13 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, SeqMap m, int
                     if (decltype(full)::value || t < rows + K - 1)
                         store_pack<T, V>(dx + (int64_t)(t - (K - 1)) * a.ldo + c, acc[0]);
                 }
+                if (decltype(full)::value || t < rows) {   // the next piece counts the rest
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    if (!decltype(full)::value) g[e] = t < rows ? g[e] : 0.0f;   // the next piece counts the rest
-                    db[e] += g[e];
+                    for (int e = 0; e < V; ++e) {
+                        db[e] += g[e];
 #pragma unroll
-                    for (int k = 0; k < K; ++k) dw[k][e] = fmaf(g[e], win[k][e], dw[k][e]);
+                        for (int k = 0; k < K; ++k) dw[k][e] = fmaf(g[e], win[k][e], dw[k][e]);
+                    }
                 }
                 shift<K, V>(win);
             }

@@ -106,3 +106,29 @@ def test_scan_infinite_inputs(S, N, layout):  # noqa: F811
     for key in g:
         finite_or_equal(key, f64(getattr(d, key)), g[key], m[key], dtype if key in ("du", "ddt", "dz", "dB", "dC") else "f32",
                         scan_k(ref[1], ref[7], ref[2], True, {"dB": D, "dC": D}.get(key, N)))
+
+
+@pytest.mark.parametrize("K", [2, 3, 4])
+@pytest.mark.parametrize("n", [[3], [40], [16, 5, 33]])
+def test_conv_infinite_inputs(S, K, n):  # noqa: F811
+    """An infinite x without an activation: infinities in the dw of the taps that
+    meet it and in y, nothing elsewhere.  In one channel it is a sequence's last
+    row, in one the first after 16 rows (a piece), in one the first of all."""
+    say("conv inf", K, n)
+    rows, D, cu = sum(n), 5, np.concatenate([[0], np.cumsum(n)])
+    r = rng(22, K, rows)
+    x, dy, w, b = r.normal(size=(rows, D)), r.normal(size=(rows, D)), r.normal(size=(D, K)), r.normal(size=D)
+    x, dy, w, b = dev(x), dev(dy), dev(w), dev(b)
+    x[n[0] - 1, 0] = x[min(16, rows - 1), 1] = float("inf")
+    x[0, 3] = -float("inf")
+    where, st = so.spans(rows, cu), np.zeros((len(n), K - 1, D))
+    cud = torch.from_numpy(cu.astype(np.int32)).cuda()
+    with np.errstate(invalid="ignore"):
+        y, _ = so.causal_conv(f64(x), f64(w), f64(b), False, st, where)
+        mass, _ = so.causal_conv(np.abs(f64(x)), np.abs(f64(w)), np.abs(f64(b)), False, st, where)
+        g, m = so.causal_conv_bwd(f64(dy), f64(x), f64(w), f64(b), False, st, where)
+    assert np.isinf(g[1]).any() and not np.isnan(g[1]).any() and np.isfinite(g[1][[2, 4]]).all()
+    finite_or_equal("y", f64(S.causal_conv_fwd(x, w, b, silu=False, cu_seqlens=cud)), y, mass, "f32", 12)
+    d = S.causal_conv_bwd(dy, x, w, b, silu=False, cu_seqlens=cud)
+    for name, t, ref, ma, k in zip(("dx", "dw", "db"), d, g, m, (24 + K, 24 + 64, 24 + 64)):
+        finite_or_equal(name, f64(t), ref, ma, "f32", k)
