@@ -95,7 +95,6 @@ struct ConvStepArgs {
 };
 hipError_t launch_conv_step(const ConvStepArgs& a, hipStream_t s);
 
-constexpr int kScanMaxN = 64;
 // Rows between the states a training pass keeps: the piece of the backward
 // kernel, 16 lanes of 4 rows.
 constexpr int kScanKeep = 64;

@@ -22,7 +22,6 @@ import torch
 
 from . import cfc as _cfc
 
-MAX_N = 64
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 _P = ctypes.c_void_p
@@ -271,7 +270,7 @@ def dropout_fwd(x, p, seed, offset=0, residual=None, y=None):
     """y = residual + keep * x / (1 - p).  What is kept follows from seed, offset
     and an element's place alone; a call uses ceil(numel / 4) offsets."""
     px, ldx = _rows(x, "x")
-    C, dev = x.shape[-1], x.device
+    C = x.shape[-1]
     seed, offset = _philox_key(seed, offset)
     pr, ldr = (None, 0) if residual is None else _rows(residual, "residual", x)
     y, py, ldy = _out(y, "y", x)
@@ -282,7 +281,7 @@ def dropout_fwd(x, p, seed, offset=0, residual=None, y=None):
 def dropout_bwd(dy, p, seed, offset=0, dx=None):
     """dx = keep * dy / (1 - p) with the forward pass's p, seed and offset."""
     pdy, lddy = _rows(dy, "dy")
-    C, dev = dy.shape[-1], dy.device
+    C = dy.shape[-1]
     seed, offset = _philox_key(seed, offset)
     dx, pdx, lddx = _out(dx, "dx", dy)
     _call("seq_dropout_bwd", dy, pdy, lddy, pdx, lddx, dy.numel() // C if C else 0, C, p, seed, offset, _TYPES[dy.dtype])
@@ -303,7 +302,7 @@ def causal_conv_fwd(x, w, b=None, silu=True, state=None, cu_seqlens=None, y=None
     [S, K - 1, D]: the inputs before each sequence (zeros if None); `state_out`
     of that shape gets the last K - 1, which causal_conv_step carries on."""
     px, ldx = _rows(x, "x")
-    D, dev = x.shape[-1], x.device
+    D = x.shape[-1]
     K, pw, pb = _taps(w, b, D, x)
     S, total, L, cu = _seqs(x, cu_seqlens)
     y, py, ldy = _out(y, "y", x)
@@ -339,7 +338,6 @@ def causal_conv_step(x, state, w, b=None, silu=True, y=None):
     if x.dim() != 2:
         raise ValueError("x is [S, D]")
     S, D = x.shape
-    dev = x.device
     K, pw, pb = _taps(w, b, D, x)
     if state is None:
         raise TypeError("state must be a tensor")
@@ -388,7 +386,7 @@ def _scan_args(u, dt, A, B, C, skip, z, dt_bias, softplus, h0, cu_seqlens):
     pu, ldu = _rows(u, "u")
     pdt, lddt = _rows(dt, "dt", u)
     pz, ldz = (None, 0) if z is None else _rows(z, "z", u)
-    D, dev = u.shape[-1], u.device
+    D = u.shape[-1]
     if not isinstance(A, torch.Tensor) or A.dim() != 2:
         raise ValueError("A is [N, D]")
     N = A.shape[0]
@@ -458,7 +456,6 @@ def selective_scan_step(h, u, dt, A, B, C, skip=None, z=None, dt_bias=None, soft
     if u.dim() != 2:
         raise ValueError("u is [S, D]")
     S, D = u.shape
-    dev = u.device
     pdt, lddt = _rows(dt, "dt", u)
     pz, ldz = (None, 0) if z is None else _rows(z, "z", u)
     if not isinstance(A, torch.Tensor) or A.dim() != 2:
