@@ -6,11 +6,13 @@ Rows x [S, L, C] (or packed [T, C] with cu_seqlens).  W_in gives the
 convolution's input and the scan's gate (halves of one buffer); the
 convolution's output u gives, through W_x, a low-rank step size and the scan's
 input and output weights B and C.  The projections are mlp_linear_*, the rest
-are the operators of recurrent_cell_amd.seq; nothing here computes on its own
-but A = -exp(A_log) and its gradient.
+are the operators of recurrent_cell_amd.seq.  Torch's own elementwise kernels
+form A = -exp(A_log) (for every call, single tokens too) and its gradient, the
+residual sums of prefill, step and backward, u's gradient from its two uses, and
+the copies that bring W_x's parts side by side.
 
 forward / backward are a training pass, prefill / step serve the same weights:
-a prompt in one pass, then a token at a time.
+a whole prompt in one pass from empty states, then a token at a time.
 """
 import math
 from dataclasses import dataclass

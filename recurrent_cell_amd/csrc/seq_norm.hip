@@ -21,11 +21,12 @@ namespace {
 // the W lanes that share it (16 or 32 lanes, one wavefront, four or eight), so x
 // is read once, and the variance is the mean square of the centred values (two
 // passes over registers, no cancellation).  Workers walk the rows with a
-// stride; the next row's loads are issued before the present row's sums; w and b
-// come from the caches (kept in registers they cost half the wavefronts per
-// SIMD: 44 us against 31 at [16384, 2048] bf16, where a copy of that size takes
-// 28).  Bound by memory: 134 MB in 31 us, 4.3 TB/s; short rows by latency
-// ([2048, 128] f32: 3 us).
+// stride; where one has a next row (the grid stops at 4,096 workgroups: more than
+// 16,384 rows of a wavefront each), its loads are issued before the present row's
+// sums.  With a row per worker, as at [16384, 2048], the registers for it buy
+// nothing.  w and b come from the caches (kept in registers they cost half the
+// wavefronts per SIMD: 44 us against 31 at [16384, 2048] bf16).  Bound by memory:
+// 134 MB in 31 us, 4.3 TB/s; short rows by latency ([2048, 128] f32: 3 us).
 // ---------------------------------------------------------------------------
 template <int W>
 __device__ __forceinline__ float worker_sum(float x, float (*red)[W >= 64 ? W / 64 : 1], int& turn)

@@ -150,8 +150,10 @@ __device__ __forceinline__ void batch_delta(float (&o)[kBatch], const T (&qt)[kB
 // A lane is a channel with its NS states in registers; B or C is the same for
 // every lane and read from LDS as a broadcast.  The next batch's loads are
 // issued before the present one's rows; rows past the end of the piece run
-// with delta = 0 and an input of 0, which change nothing.  Bound by the vector
-// ALU, 82 % busy: [4, 4096, 2048] bf16 with 16 states 120 us; [4, 2048, 1024] 38.
+// with delta = 0 and an input of 0, which change nothing.  With four wavefronts
+// per SIMD bound by the vector ALU, 82 % busy: [4, 4096, 2048] bf16 with 16 states
+// 117 us.  With the two that [4, 2048, 1024] has it is 52 % busy, and what the two
+// wait for shows: 38 us.
 // ---------------------------------------------------------------------------
 template <typename T, int NS, bool REV>
 __global__ __launch_bounds__(256) void scan_state_kernel(ScanArgs a, SeqMap m, int slots)
@@ -310,9 +312,10 @@ __device__ __forceinline__ float join_own(const ScanArgs& a, const SeqMap& m, co
 
 // ---------------------------------------------------------------------------
 // Main forward pass: a lane is a channel, its NS states in registers, one row
-// at a time.  Per row and state one exp2 and four products or sums.  Bound by the
-// vector ALU, 83 % busy: [4, 4096, 2048] bf16 with 16 states 158 us, of whose 118
-// vector instructions per row 80 are the recurrence; [4, 2048, 1024] 48 us.
+// at a time.  Per row and state one exp2 and four products or sums.  With four
+// wavefronts per SIMD bound by the vector ALU, 84 % busy: [4, 4096, 2048] bf16 with
+// 16 states 158 us, of whose 119 vector instructions per row 80 are the
+// recurrence.  With two ([4, 2048, 1024]) 57 % busy: 48 us.
 // Where N is not NS (FULL), a row ends with its last state: the B and C of 0 past
 // it would turn an infinite input into NaN, which y would take.  At
 // [4, 2048, 1024] with 11 states the forward pass takes 84.5 us so, 85.5 over all
