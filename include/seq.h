@@ -111,7 +111,10 @@ int seq_causal_conv_step(const void* x, int64_t ldx, void* state, const float* w
  * and h before a sequence's first row is h0 [n_seq, N, D], or 0.  States decay:
  * A <= 0 and delta >= 0.  Growth is computed too while exp(A times the sum of
  * delta over any run of rows) stays finite in fp32: products of decays over
- * many rows are formed apart from the states they act on. */
+ * many rows are formed apart from the states they act on.  dt = -inf is a row
+ * that keeps the state (delta = 0), A = -inf a state that keeps nothing.  An
+ * infinite state stays infinite while its decay over 64 rows does not round to
+ * 0, and is NaN after rows where it does. */
 typedef struct seq_scan {
     const void* u;  int64_t ldu;    /* [rows, D] */
     const void* dt; int64_t lddt;   /* [rows, D] */
