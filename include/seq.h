@@ -113,8 +113,8 @@ int seq_causal_conv_step(const void* x, int64_t ldx, void* state, const float* w
  * delta over any run of rows) stays finite in fp32: products of decays over
  * many rows are formed apart from the states they act on.  dt = -inf is a row
  * that keeps the state (delta = 0), A = -inf a state that keeps nothing.  An
- * infinite state stays infinite while its decay over 64 rows does not round to
- * 0, and is NaN after rows where it does. */
+ * infinite state stays infinite while its decay over the rows that follow does
+ * not round to 0, and may be NaN where it does. */
 typedef struct seq_scan {
     const void* u;  int64_t ldu;    /* [rows, D] */
     const void* dt; int64_t lddt;   /* [rows, D] */
